@@ -134,9 +134,8 @@ def _tables_state(case, g):
         live = (col >= lo[:, None]) & (col < hi[:, None])
         owned = torch.where(live, order[at.clamp(0, pages - 1)], -1).int().contiguous()
         head = int(torch.randint(0, 4 * pages, (1,), generator=g, device="cuda"))
-        # twice the pages: room to return pages while the step's new ones are still being read
-        ring = torch.full((2 * pages,), -1, dtype=torch.int32, device="cuda")
-        ring[(head + torch.arange(pages - used, device="cuda")) % (2 * pages)] = order[used:]
+        ring = torch.full((pages,), -1, dtype=torch.int32, device="cuda")
+        ring[(head + torch.arange(pages - used, device="cuda")) % pages] = order[used:]
         pool = torch.tensor([head, head + pages - used], dtype=torch.int64, device="cuda")
         state["groups"].append({"ratio": ratio, "window": window, "owned": owned, "ring": ring, "pool": pool, "num_pages": pages})
     return state

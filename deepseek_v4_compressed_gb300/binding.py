@@ -559,9 +559,10 @@ def _raw_stream(stream, device):
 class TableGroup:
     """One cache group of a batch (dsv4_table_group): ratio tokens per entry,
     a window in tokens (0: none), the pages of its cache; owned (in and out)
-    and table (out) int32 [num_seqs, stride], ring int32 [ring_size] (twice
-    the pages always has room), pool_in / pool_out int64 [2] = (head, tail),
-    slots int64 [max_tokens] or None."""
+    and table (out) int32 [num_seqs, stride], ring int32 [ring_size] (as many
+    as pages always have room; with twice as many a step can be built again),
+    pool_in / pool_out int64 [2] = (head, tail), slots int64 [max_tokens] or
+    None."""
 
     def __init__(self, ratio, num_pages, owned, table, ring, pool_in, pool_out, window=0, slots=None):
         self.ratio, self.window, self.num_pages = int(ratio), int(window), int(num_pages)

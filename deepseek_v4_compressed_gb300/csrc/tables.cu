@@ -16,6 +16,8 @@
 // where writing the tables and reading the pages held takes 4.6 us).
 #include <limits.h>
 
+#include <type_traits>
+
 #include "dsv4_common.cuh"
 #include "host_once.h"
 #include "tmap.h"
@@ -144,10 +146,16 @@ __device__ __forceinline__ unsigned ring_base(long long x, unsigned size)
     return static_cast<unsigned>(x % static_cast<long long>(size));
 }
 
+// What a step does with a group's ring: nothing; every CTA with its own rows'
+// pages; or one CTA with all of them, where returned pages go to places that the
+// step's taken ones are read from.
+enum { kRefused = 0, kShared = 1, kAlone = 2 };
+
 struct TabShared {
     int total[2 * kTabGroups + 1];                 // taken and returned pages by group, tokens (at most max_tokens + 1)
     unsigned head[kTabGroups], tail[kTabGroups];   // ring positions
-    int ok[kTabGroups];
+    int ok[kTabGroups];                            // kRefused, kShared or kAlone
+    unsigned alone;                                // bit g: group g is kAlone
     unsigned next;                                 // the next of the CTA's units of old entries
 };
 
@@ -198,6 +206,66 @@ __device__ __forceinline__ TabUnit table_unit(const TabParams& P, unsigned u)
     t.j0 = static_cast<int>(u - row * G.segs) * kTabSeg;
     t.j1 = min(t.j0 + kTabSeg, G.stride);
     return t;
+}
+
+// The pages that a step takes from and returns to the ring of group g, by one CTA
+// (all of its threads): every taken page is read, into `owned`, the table and the
+// slot map, ahead of any write to the ring.  Only a windowed group comes here, when
+// its chunks pass through more pages than are in use (the first prompts of an idle
+// service).  Out of line: other steps do not fetch it, and what they pay for the
+// possibility is 0.0, 0.3 and 0.3 us at 32, 200 and 2048 sequences.  A step that
+// comes here takes longer: about 12 us for 170 pages of 21,000 new tokens.
+__device__ __noinline__ void ring_alone(const TabParams& P, const TabShared& S, int g, const int* len_c, const int* len_n,
+                                        const int* take_off, const int* give_off, const int* tok_off, int real)
+{
+    const TabGroup& G = P.g[g];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int bad = 0;
+    for (unsigned u = warp; u < G.units; u += kTabWarps) {
+        const int s = u / G.segs, j0 = static_cast<int>(u % G.segs) * kTabSeg;
+        const int c = len_c[s], n = max(len_n[s], 0);
+        const int before = pages_of(c, G.shift), after = pages_of(c + n, G.shift);
+        const int a = max(j0, before), b = min(min(j0 + kTabSeg, G.stride), after);
+        const long long row = static_cast<long long>(s) * G.stride;
+        for (int k0 = a; k0 < b; k0 += 32) {
+            const int k = k0 + lane;
+            int v = -1;
+            if (k < b) {
+                v = G.ring[ring_at(S.head[g] + take_off[s], k - before, G.ring_size)];
+                G.owned[row + k] = v;
+                if (v < 0 || v >= G.num_pages) {
+                    v = -1;
+                    bad = 1;
+                }
+                G.table[row + k] = v;
+            }
+            if (G.slots == nullptr) continue;
+            // the tokens that complete the entries of 32 pages, a page at a time
+            for (int i = 0; i < min(32, b - k0); ++i) {
+                const long long page = __shfl_sync(0xffffffffu, v, i);
+#pragma unroll
+                for (int r = lane; r < kPage; r += 32) {
+                    const long long off = ((((static_cast<long long>(k0) + i) * kPage + r + 1) << G.shift) - 1) - c;
+                    if (off < 0 || off >= n || tok_off[s] + off >= real) continue;
+                    G.slots[tok_off[s] + off] = page < 0 ? -1 : page * kPage + r;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    for (unsigned u = warp; u < G.units; u += kTabWarps) {
+        const int s = u / G.segs, j0 = static_cast<int>(u % G.segs) * kTabSeg;
+        SeqLen q;
+        q.c = len_c[s];
+        q.done = len_n[s] < 0;
+        q.n = max(len_n[s], 0);
+        int lo, before, after, gone;
+        seq_pages(G.shift, G.window, q, lo, before, after, gone);
+        const long long row = static_cast<long long>(s) * G.stride;
+        for (int k = max(j0, lo) + lane; k < min(j0 + kTabSeg, gone); k += 32)
+            G.ring[ring_at(S.tail[g] + give_off[s], k - lo, G.ring_size)] = G.owned[row + k];
+    }
+    if (bad) flag(P.status, DSV4_DEV_BAD_PAGE);
 }
 
 __global__ void __launch_bounds__(kTabThreads) batch_tables_kernel(const __grid_constant__ TabParams P)
@@ -273,8 +341,7 @@ __global__ void __launch_bounds__(kTabThreads) batch_tables_kernel(const __grid_
     }
 
     // ---- the tables' old entries: one warp per unit, 512 entries at a time, all
-    // their reads ahead of any write.  New entries stay -1 until their pages are
-    // known.
+    // their reads ahead of any write.  New entries are left to who knows their pages.
     while (true) {
         unsigned i = 0;
         if (lane == 0) i = atomicAdd(&S.next, 1u);
@@ -284,6 +351,7 @@ __global__ void __launch_bounds__(kTabThreads) batch_tables_kernel(const __grid_
         const TabGroup& G = P.g[t.g];
         const SeqLen q = seq_len(R, P.computed[t.s], P.fresh[t.s]);
         const int before = q.done ? 0 : pages_of(q.c, G.shift), lo = first_live(q.c, G.window);
+        const int after = q.done ? 0 : pages_of(q.c + q.n, G.shift);
         const int* owned = G.owned + static_cast<long long>(t.s) * G.stride;
         int* table = G.table + static_cast<long long>(t.s) * G.stride;
         int bad = 0;
@@ -292,7 +360,8 @@ __global__ void __launch_bounds__(kTabThreads) batch_tables_kernel(const __grid_
             bad = 1;
             return -1;
         };
-        if (G.vec) {
+        // 16 bytes a lane; `fresh`: the row has new entries
+        auto by_chunks = [&](auto fresh) {
             for (int j = t.j0; j < t.j1; j += 512) {
                 int4 v[4];
 #pragma unroll
@@ -311,36 +380,70 @@ __global__ void __launch_bounds__(kTabThreads) batch_tables_kernel(const __grid_
                         v[i].z = k + 2 >= lo && k + 2 < before ? known(v[i].z) : -1;
                         v[i].w = k + 3 >= lo && k + 3 < before ? known(v[i].w) : -1;
                     }
-                    if (k < t.j1) *reinterpret_cast<int4*>(table + k) = v[i];
+                    if (k < t.j1 && (!fresh.value || k + 3 < before || k >= after)) *reinterpret_cast<int4*>(table + k) = v[i];
                 }
             }
-        } else {
+        };
+        // Each of the two loops once more for rows with new entries, not once for
+        // both: the conditions cost 0.1 to 0.3 us at 32 and 2048 sequences.
+        if (G.vec && after == before) {
+            by_chunks(std::false_type{});
+        } else if (G.vec) {
+            by_chunks(std::true_type{});
+            // what shares a chunk with the first or the last new entry
+            const int k = ((lane < 4 ? before : after) & ~3) + (lane & 3);
+            if (lane < 8 && k >= t.j0 && k < t.j1 && (lane < 4 ? k < before : k >= after))
+                table[k] = k >= lo && k < before ? known(owned[k]) : -1;
+        } else if (after == before) {
             for (int j = t.j0 + lane; j < t.j1; j += 32) table[j] = j >= lo && j < before ? known(owned[j]) : -1;
+        } else {
+#pragma unroll 1
+            for (int j = t.j0 + lane; j < t.j1; j += 128) {
+                int v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int k = j + 32 * i;
+                    v[i] = k >= lo && k < min(t.j1, before) ? owned[k] : -1;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int k = j + 32 * i;
+                    if (k < t.j1 && (k < before || k >= after)) table[k] = k >= lo && k < before ? known(v[i]) : -1;
+                }
+            }
         }
         if (bad) flag(P.status, DSV4_DEV_BAD_PAGE);
     }
 
     __syncthreads();
-    // ---- the pools: a group that cannot take or return all its pages does neither
-    if (tid < ng) {
-        const TabGroup& G = P.g[tid];
-        const long long taken = S.total[2 * tid], freed = S.total[2 * tid + 1];
-        const long long avail = tail - head;
-        const bool ok = head >= 0 && tail >= head && avail <= G.ring_size && taken <= avail &&
-                        avail + freed <= static_cast<long long>(G.ring_size) && tail <= LLONG_MAX - freed;
-        S.ok[tid] = ok;
-        // an empty ring is never read or written: nothing to take, nothing to return
-        S.head[tid] = ok && G.ring_size ? ring_base(head, G.ring_size) : 0;
-        S.tail[tid] = ok && G.ring_size ? ring_base(tail, G.ring_size) : 0;
-        if (first) {
-            G.pool_out[0] = ok ? head + taken : head;
-            G.pool_out[1] = ok ? tail + freed : tail;
-            if (!ok) flag(P.status, DSV4_DEV_BAD_PAGE);
+    // ---- the pools: a group that cannot take or return all its pages does neither.
+    // The places of the pages that it takes are free for those that it returns.
+    if (warp == 0) {
+        bool over = false;
+        if (lane < ng) {
+            const TabGroup& G = P.g[lane];
+            const long long taken = S.total[2 * lane], freed = S.total[2 * lane + 1];
+            const long long avail = tail - head, size = G.ring_size;
+            const bool ok = head >= 0 && tail >= head && avail <= size && taken <= avail &&
+                            avail - taken + freed <= size && tail <= LLONG_MAX - freed;
+            over = ok && avail + freed > size;
+            S.ok[lane] = !ok ? kRefused : (over ? kAlone : kShared);
+            // an empty ring is never read or written: nothing to take, nothing to return
+            S.head[lane] = ok && G.ring_size ? ring_base(head, G.ring_size) : 0;
+            S.tail[lane] = ok && G.ring_size ? ring_base(tail, G.ring_size) : 0;
+            if (first) {
+                G.pool_out[0] = ok ? head + taken : head;
+                G.pool_out[1] = ok ? tail + freed : tail;
+                if (!ok) flag(P.status, DSV4_DEV_BAD_PAGE);
+            }
         }
+        const unsigned alone = __ballot_sync(0xffffffffu, over);
+        if (lane == 0) S.alone = alone;
     }
     if (first && tid == 0 && S.total[2 * ng] > cap) flag(P.status, DSV4_DEV_BAD_INDEX);
     __syncthreads();
 
+    const unsigned alone = S.alone;
     // ---- token rows, 32 a warp, from the last warps on (the first ones have more
     // table rows to go on with)
     const int real = min(tok_off[nseq], cap);              // offsets past max_tokens only drop tokens
@@ -357,7 +460,7 @@ __global__ void __launch_bounds__(kTabThreads) batch_tables_kernel(const __grid_
             c = len_c[s];
             p = c + (t - tok_off[s]);
         }
-        int page[kTabGroups];                      // -2: the token completes no entry
+        int page[kTabGroups];                      // -2: the token completes no entry; -3: ring_alone's
 #pragma unroll
         for (int g = 0; g < kTabGroups; ++g) {
             page[g] = -2;
@@ -367,7 +470,9 @@ __global__ void __launch_bounds__(kTabThreads) batch_tables_kernel(const __grid_
             const int j = (p >> G.shift) / kPage, before = pages_of(c, G.shift);
             page[g] = -1;
             if (j < before) page[g] = G.owned[static_cast<long long>(s) * G.stride + j];
-            else if (S.ok[g]) page[g] = G.ring[ring_at(S.head[g] + counts[2 * g * npad + s], j - before, G.ring_size)];
+            else if (S.ok[g] == kAlone) page[g] = -3;
+            else if (S.ok[g] == kShared)
+                page[g] = G.ring[ring_at(S.head[g] + counts[2 * g * npad + s], j - before, G.ring_size)];
         }
         if (P.positions) P.positions[t] = p;
         if (P.seqs) P.seqs[t] = s;
@@ -376,6 +481,7 @@ __global__ void __launch_bounds__(kTabThreads) batch_tables_kernel(const __grid_
         for (int g = 0; g < kTabGroups; ++g) {
             if (g >= ng || P.g[g].slots == nullptr) continue;
             const TabGroup& G = P.g[g];
+            if (page[g] == -3) continue;
             long long slot = -1;
             if (page[g] >= 0 && page[g] < G.num_pages)
                 slot = static_cast<long long>(page[g]) * kPage + (p >> G.shift) % kPage;
@@ -394,15 +500,18 @@ __global__ void __launch_bounds__(kTabThreads) batch_tables_kernel(const __grid_
         q.n = max(len_n[t.s], 0);
         int lo, before, after, gone;
         seq_pages(G.shift, G.window, q, lo, before, after, gone);
-        if (!S.ok[t.g]) {
-            // the new entries stay unmapped
+        if (S.ok[t.g] == kAlone) continue;
+        int* owned = G.owned + static_cast<long long>(t.s) * G.stride;
+        int* table = G.table + static_cast<long long>(t.s) * G.stride;
+        if (S.ok[t.g] == kRefused) {
+            // the new entries are unmapped
+#pragma unroll 1
+            for (int j = max(t.j0, before) + lane; j < min(t.j1, after); j += 32) table[j] = -1;
             if (after > before && lane == 0 && t.j0 == 0) flag(P.status, DSV4_DEV_BAD_PAGE);
             continue;
         }
         const unsigned take = S.head[t.g] + counts[2 * t.g * npad + t.s],
                        give = S.tail[t.g] + counts[(2 * t.g + 1) * npad + t.s];
-        int* owned = G.owned + static_cast<long long>(t.s) * G.stride;
-        int* table = G.table + static_cast<long long>(t.s) * G.stride;
         int bad = 0;
         // entries [a, b) of the unit that are taken or returned, four reads ahead
         const int a = max(t.j0, gone > lo ? min(lo, before) : before);
@@ -430,6 +539,11 @@ __global__ void __launch_bounds__(kTabThreads) batch_tables_kernel(const __grid_
         }
         if (bad) flag(P.status, DSV4_DEV_BAD_PAGE);
     }
+    // ---- rings that one CTA takes from and returns to
+#pragma unroll 1
+    for (int g = 0; alone >> g; ++g)
+        if ((alone >> g & 1) && blockIdx.x == gridDim.x - 1 - g % gridDim.x)
+            ring_alone(P, S, g, len_c, len_n, counts + 2 * g * npad, counts + (2 * g + 1) * npad, tok_off, real);
     if (first && P.offsets)
         for (int s = tid; s <= nseq; s += kTabThreads) P.offsets[s] = min(tok_off[s], cap);
     // the kernels behind this one may read the tables before their own wait

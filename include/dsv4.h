@@ -648,10 +648,12 @@ dsv4_status dsv4_stream_gate(const dsv4_gate_args* args, dsv4_stream_t stream);
  *     group's cache, counted over all its pages ([MLA-to-CSA] 6.3).
  * The pool is a ring of ring_size page ids with two running counters
  * pool = {head, tail}: the ids at [head, tail) modulo ring_size are free.
- * Returned pages are written behind tail while the taken ones are read, so
- * the ring needs room for both: ring_size = 2 * num_pages always has it.
- * The call reads pool_in and writes pool_out; two sets of counters let the
- * same step be built again from the same inputs with the same result.
+ * Taken ids leave the ring, returned ones are written behind tail, also where
+ * taken ones stood: tail - head - taken + returned ids have to fit, which
+ * ring_size = num_pages always has room for.  The call reads pool_in and
+ * writes pool_out; two sets of counters let the same step be built again from
+ * the same inputs with the same result, as long as no taken id was written
+ * over (tail - head + returned <= ring_size; 2 * num_pages always has that).
  * Everything is in a fixed order: same inputs, same bytes.
  *
  * Refused on the device (bit set, sequence treated as finished without pages

@@ -504,9 +504,10 @@ __global__ void __launch_bounds__(kTabThreads) batch_tables_kernel(const __grid_
         int* owned = G.owned + static_cast<long long>(t.s) * G.stride;
         int* table = G.table + static_cast<long long>(t.s) * G.stride;
         if (S.ok[t.g] == kRefused) {
-            // the new entries are unmapped
+            // the new entries are unmapped, also for a step that goes on from here: what
+            // `owned` has there may be another sequence's by now
 #pragma unroll 1
-            for (int j = max(t.j0, before) + lane; j < min(t.j1, after); j += 32) table[j] = -1;
+            for (int j = max(t.j0, before) + lane; j < min(t.j1, after); j += 32) owned[j] = table[j] = -1;
             if (after > before && lane == 0 && t.j0 == 0) flag(P.status, DSV4_DEV_BAD_PAGE);
             continue;
         }

@@ -213,7 +213,7 @@ __device__ __forceinline__ TabUnit table_unit(const TabParams& P, unsigned u)
 // slot map, ahead of any write to the ring.  Only a windowed group comes here, when
 // its chunks pass through more pages than are in use (the first prompts of an idle
 // service).  Out of line: other steps do not fetch it, and what they pay for the
-// possibility is 0.0, 0.3 and 0.3 us at 32, 200 and 2048 sequences.  A step that
+// possibility is 0.1, 0.0 and 0.4 us at 32, 200 and 2048 sequences.  A step that
 // comes here takes longer: about 12 us for 170 pages of 21,000 new tokens.
 __device__ __noinline__ void ring_alone(const TabParams& P, const TabShared& S, int g, const int* len_c, const int* len_n,
                                         const int* take_off, const int* give_off, const int* tok_off, int real)
@@ -262,8 +262,11 @@ __device__ __noinline__ void ring_alone(const TabParams& P, const TabShared& S, 
         int lo, before, after, gone;
         seq_pages(G.shift, G.window, q, lo, before, after, gone);
         const long long row = static_cast<long long>(s) * G.stride;
-        for (int k = max(j0, lo) + lane; k < min(j0 + kTabSeg, gone); k += 32)
-            G.ring[ring_at(S.tail[g] + give_off[s], k - lo, G.ring_size)] = G.owned[row + k];
+        for (int k = max(j0, lo) + lane; k < min(j0 + kTabSeg, gone); k += 32) {
+            const int v = G.owned[row + k];
+            G.ring[ring_at(S.tail[g] + give_off[s], k - lo, G.ring_size)] = v;
+            if (v < 0 || v >= G.num_pages) bad = 1;
+        }
     }
     if (bad) flag(P.status, DSV4_DEV_BAD_PAGE);
 }
@@ -355,8 +358,9 @@ __global__ void __launch_bounds__(kTabThreads) batch_tables_kernel(const __grid_
         const int* owned = G.owned + static_cast<long long>(t.s) * G.stride;
         int* table = G.table + static_cast<long long>(t.s) * G.stride;
         int bad = 0;
+        // (one comparison: negative ids are large ones)
         auto known = [&](int v) {
-            if (v >= 0 && v < G.num_pages) return v;
+            if (static_cast<unsigned>(v) < static_cast<unsigned>(G.num_pages)) return v;
             bad = 1;
             return -1;
         };
@@ -530,11 +534,12 @@ __global__ void __launch_bounds__(kTabThreads) batch_tables_kernel(const __grid_
             for (int i = 0; i < 4; ++i) {
                 const int k = j + 32 * i;
                 if (k >= b || (k < before && (k < lo || k >= gone))) continue;
-                if (k >= lo && k < gone) G.ring[ring_at(give, k - lo, G.ring_size)] = v[i];
+                if (k < gone) G.ring[ring_at(give, k - lo, G.ring_size)] = v[i];
+                // all of these are at lo or behind: a returned one is checked as well
+                const bool live = static_cast<unsigned>(v[i]) < static_cast<unsigned>(G.num_pages);
+                if (!live) bad = 1;
                 if (k < before) continue;
                 owned[k] = v[i];
-                const bool live = k >= lo && v[i] >= 0 && v[i] < G.num_pages;
-                if (k >= lo && !live) bad = 1;
                 table[k] = live ? v[i] : -1;
             }
         }

@@ -667,7 +667,8 @@ dsv4_status dsv4_stream_gate(const dsv4_gate_args* args, dsv4_stream_t stream);
  * step is to be built again once there are pages; a call whose lengths lie
  * behind it finds none for it (DSV4_DEV_BAD_PAGE), and what it would have
  * returned stays out of the pool.  A page id outside [0, num_pages) shows as
- * -1 in tables and slots (DSV4_DEV_BAD_PAGE).
+ * -1 in tables and slots and goes back to the pool as it is (both
+ * DSV4_DEV_BAD_PAGE).
  *
  * computed_dev, new_dev: int32 [num_seqs]; offsets_dev: int32 [num_seqs + 1];
  * ctx_len_dev: int32 [num_seqs]; positions_dev, seqs_dev, row_ctx_dev: int32

@@ -75,3 +75,45 @@ def test_a_refused_step_leaves_the_entries_held_before():
         n, lo = pages_of(300, b["ratio"]), first_live(300, b["window"])
         assert torch.equal(g["owned"][:, :n], h[:, :n]) and torch.equal(g["table"][:, lo:n], h[:, lo:n])
         assert g["table"][:, :lo].eq(-1).all() and g["table"][:, n:].eq(-1).all()
+
+
+@pytest.mark.parametrize("kind", ["swa", "full", "c4"])
+@pytest.mark.parametrize("value", [-1, 60, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("busy", [False, True])
+def test_a_finished_sequence_with_an_id_out_of_range(kind, value, busy):
+    """What it returns is flagged; `busy`: beside a prompt whose pages pass
+    through the same places of the ring."""
+    s = Service(2, (kind,), spare=60)
+    assert s.step([0, 0], [1100, 0]) == 0
+    g, (ratio, window) = s.d.groups[0], (s.b.groups[0]["ratio"], s.b.groups[0]["window"])
+    if busy:
+        # as many places as pages: the prompt takes all that are free
+        ring, pool = g["ring"].cpu().tolist(), g["pool"].cpu().tolist()
+        free = [ring[p % len(ring)] for p in range(*pool)]
+        size = len(free) + pages_of(1100, ratio) - first_live(1100, window)
+        cut = torch.full((size,), -7, dtype=torch.int32, device="cuda")
+        cut[:len(free)] = torch.tensor(free, dtype=torch.int32)
+        g["ring"] = cut
+        g["pool"].copy_(torch.tensor([0, len(free)]))
+        s.d.tables = B.BatchTables([B.TableGroup(ratio=ratio, window=window, num_pages=60, owned=g["owned"], table=g["table"], ring=cut, pool_in=g["pool"],
+                                                 pool_out=g["pool_out"], slots=g["slots"])], num_seqs=2, max_tokens=2048, status=s.d.status, **s.d.out)
+    last = pages_of(1100, ratio) - 1
+    old = g["owned"][0, first_live(1100, window):last + 1].tolist()
+    g["owned"][0, last] = value
+    before = g["pool"].cpu().tolist()
+    new = [-1, 1900 if busy and kind == "swa" else 0]
+    assert s.step([1100, 0], new, advance=False) == B.DEV_BAD_PAGE
+    head, tail = g["pool_out"].cpu().tolist()
+    assert head == before[0] + pages_of(max(new[1], 0), ratio)
+    back = [int(g["ring"][p % g["ring"].numel()]) for p in range(before[1], before[1] + len(old))]
+    assert back == old[:-1] + [value]
+    g["owned"][0, last] = old[-1]
+    if not busy:
+        assert s.step([1100, 0], new, advance=False) == 0
+
+
+def test_a_live_sequences_returned_id_out_of_range():
+    s = Service(1, ("swa",), spare=60)
+    assert s.step([0], [300]) == 0
+    s.d.groups[0]["owned"][0, first_live(300, 128)] = 99
+    assert s.step([300], [100]) == B.DEV_BAD_PAGE

@@ -616,6 +616,7 @@ class BatchTables:
         self.groups = groups
         self._keep = (offsets, ctx_len, positions, seqs, row_ctx, status)     # the addresses stay valid
         self._shape, self._call = (a.num_seqs,), lib().dsv4_build_batch_tables
+        self.device = groups[0].pool_in.get_device()                          # of all buffers
         # the arguments around the lengths' addresses, which each call puts in
         # between: two host threads may build on two streams
         raw = bytes(a)
@@ -628,9 +629,12 @@ class BatchTables:
         dev = computed.get_device()
         if not (computed.shape == self._shape == new.shape and computed.dtype is new.dtype is torch.int32 and
                 computed.is_contiguous() and new.is_contiguous() and
-                dev == new.get_device() == torch.cuda.current_device()):
+                dev == new.get_device() == self.device == torch.cuda.current_device()):
             for t, what in ((computed, "computed"), (new, "new")):
                 _tensor(t, what, _I32, self._shape)
+            if self.device != torch.cuda.current_device():
+                raise ValueError("the tables' buffers live on cuda:%d, the current device is cuda:%d" %
+                                 (self.device, torch.cuda.current_device()))
         st = self._call(self._head + _PAIR_PACK(computed.data_ptr(), new.data_ptr()) + self._tail,
                         torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
         if st:

@@ -1222,7 +1222,7 @@ extern "C" dsv4_status dsv4_fp8_block_matmul(const dsv4_fp8_matmul_args* a, dsv4
     P.G = a->groups;
     P.N = a->n;
     P.K = a->k;
-    P.kblocks = (a->k + 127) / 128;
+    P.kblocks = static_cast<int>((K + 127) / 128);       // 64-bit: k may be near 2^31
     P.x = static_cast<const uint8_t*>(a->x_dev);
     P.x_ts = a->x_token_stride;
     P.x_gs = a->x_group_stride;

@@ -57,7 +57,7 @@ __device__ __forceinline__ void load_chunk(const T* row, int c0, int lane, int c
 {
     const int c = VEC ? c0 + lane * kPer<T> : c0 + lane;
     constexpr int step = VEC ? 1 : kLanes<T>;
-    if (VEC && c + kPer<T> <= cols) {
+    if (VEC && kPer<T> <= cols - c) {           // (no sum: cols may be near 2^31)
         const uint4 raw = *reinterpret_cast<const uint4*>(row + c);
         const T* v = reinterpret_cast<const T*>(&raw);
 #pragma unroll
@@ -86,7 +86,7 @@ __device__ __forceinline__ void store_chunk(uint8_t* row, int c0, int lane, int 
     uint32_t w[N / 4];
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) w[i] = div.codes<N == 8 ? 1 : 2>(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-    if (VEC && c + N <= cols) {
+    if (VEC && N <= cols - c) {
         if constexpr (N == 8) *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
         else *reinterpret_cast<uint32_t*>(row + c) = w[0];
     } else {

@@ -250,7 +250,7 @@ __device__ __forceinline__ void compress_token(const CompressParams& P, const in
     const int seq = P.seqs[t];
     const int p = P.positions[t];
     if (seq < 0 || seq >= P.num_seqs || p < 0) {
-        if (threadIdx.x == 0) flag(P.status, DSV4_DEV_BAD_INDEX);
+        if (threadIdx.x == 0 && !padding_row(seq, p)) flag(P.status, DSV4_DEV_BAD_INDEX);
         return;
     }
     if (!FUSED && t > 0 && P.seqs[t - 1] == seq && P.positions[t - 1] != p - 1) {
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(D / 2) insert_rows_kernel(const float* rows, c
     const int c0 = 2 * threadIdx.x;
     const int seq = seqs[i], j = slots[i];
     if (seq < 0 || seq >= P.num_seqs || j < 0) {
-        if (threadIdx.x == 0) flag(P.status, DSV4_DEV_BAD_INDEX);
+        if (threadIdx.x == 0 && !padding_row(seq, j)) flag(P.status, DSV4_DEV_BAD_INDEX);
         return;
     }
     const float2 z = *reinterpret_cast<const float2*>(rows + static_cast<long long>(i) * D + c0);

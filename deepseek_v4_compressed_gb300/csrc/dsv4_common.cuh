@@ -22,6 +22,10 @@ constexpr int kIdxPage = DSV4_IDX_PAGE_BYTES;
 constexpr int kIdxFp4Page = DSV4_IDX_FP4_PAGE_BYTES;
 constexpr int kSwaPage = DSV4_SWA_PAGE_BYTES;
 
+// A row behind a batch's last token, as the batch tables write it (`at`: its
+// position or slot): the calls skip it, flagging nothing.
+__device__ __forceinline__ bool padding_row(int seq, int at) { return seq == -1 && at == -1; }
+
 __device__ __forceinline__ void flag(int* status, int bits)
 {
     if (status) atomicOr(status, bits);

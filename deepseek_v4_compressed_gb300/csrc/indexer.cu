@@ -447,7 +447,8 @@ indexer_logits_tc(const __grid_constant__ CUtensorMap tm_cache, const __grid_con
         if (P.row_seq) {
             sq = P.row_seq[b];
             if (sq < 0 || sq >= P.bt_rows) {
-                if (lane == 0) flag(P.status, DSV4_DEV_BAD_INDEX);
+                // (a padding row reads nothing: it has no slots)
+                if (lane == 0 && !padding_row(sq, P.ctx_len[b] - 1)) flag(P.status, DSV4_DEV_BAD_INDEX);
                 sq = 0;
             }
         }

@@ -285,6 +285,12 @@ mla_decode_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     if (P.row_seq) {
         seq = P.row_seq[b];
         if (seq < 0 || seq >= P.bt_rows) {
+            if (padding_row(seq, P.ctx_len[b] - 1)) {
+                // its whole cluster leaves the row as it was; this grid ends after the
+                // ones before it all the same
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                return;
+            }
             if (threadIdx.x == 0) flag(P.status, DSV4_DEV_BAD_INDEX);
             seq = 0;
         }
@@ -1002,7 +1008,7 @@ struct CombineParams {
 // One warp per prefill token: the valid top-k entries in order (ballot
 // compaction), then the window tokens as rows n_comp + (t - first gathered).
 // A window token outside the gathered run, a bad sequence or too short an
-// output row sets DSV4_DEV_BAD_INDEX and length -1.
+// output row sets DSV4_DEV_BAD_INDEX and length -1.  A padding row has length 0.
 __global__ void __launch_bounds__(32) combine_indices_kernel(CombineParams C)
 {
     const int t = blockIdx.x, lane = threadIdx.x;
@@ -1010,6 +1016,10 @@ __global__ void __launch_bounds__(32) combine_indices_kernel(CombineParams C)
     const int s = C.row_seq[t];
     const int len = C.topk_len[t];
     const int pos = C.pos[t];
+    if (padding_row(s, pos)) {
+        if (lane == 0) C.out_len[t] = 0;
+        return;
+    }
     bool bad = s < 0 || s >= C.num_seqs || len < 0 || len > C.topk_stride || pos < 0;
     int first = 0, seq_len = 0;
     if (!bad) {
@@ -1185,7 +1195,7 @@ extern "C" dsv4_status dsv4_sparse_mla_decode(const dsv4_plan* plan, const dsv4_
                        : cudaLaunchKernelEx(&cfg, mla_decode_tc<false>, tm_q, tm_swa, T);
     if (e == cudaSuccess && want_codes)
         e = launch_inv_rope_quant(static_cast<const uint16_t*>(a->out_dev), plan->batch, P.H, a->ctx_len_dev, true,
-                                  a->cos_sin_dev, a->max_pos, static_cast<uint8_t*>(a->out_codes_dev),
+                                  a->row_seq_dev, a->cos_sin_dev, a->max_pos, static_cast<uint8_t*>(a->out_codes_dev),
                                   a->out_scales_dev, a->status_dev, st);
     return e == cudaSuccess ? DSV4_OK : DSV4_ERR_CUDA;
 }

@@ -24,6 +24,7 @@ struct InvRopeQuantParams {
     const uint16_t* o;
     const int* pos;
     int pos_minus;                 // subtracted from pos[t]: 1 when pos holds context lengths
+    const int* row_seq;            // NULL: no padding rows
     const float* cos_sin;
     int max_pos;
     int n_heads;
@@ -47,7 +48,7 @@ __global__ void __launch_bounds__(32 * 4 * kOqRowsPerCta) inv_rope_fp8_quant_ker
     const int t = static_cast<int>(row / Q.n_heads);
     const int pos = Q.pos[t] - Q.pos_minus;
     if (pos < 0 || pos >= Q.max_pos) {
-        if (lane == 0 && blk == 0) flag(Q.status, DSV4_DEV_BAD_POSITION);
+        if (lane == 0 && blk == 0 && !(Q.row_seq != nullptr && padding_row(Q.row_seq[t], pos))) flag(Q.status, DSV4_DEV_BAD_POSITION);
         return;
     }
     const int c = blk * 128 + 4 * lane;
@@ -75,13 +76,14 @@ __global__ void __launch_bounds__(32 * 4 * kOqRowsPerCta) inv_rope_fp8_quant_ker
 }
 
 cudaError_t launch_inv_rope_quant(const uint16_t* o, int num_tokens, int n_heads, const int* pos, bool pos_is_ctx,
-                                  const float* cos_sin, int max_pos, uint8_t* codes, float* scales, int* status,
-                                  cudaStream_t stream)
+                                  const int* row_seq, const float* cos_sin, int max_pos, uint8_t* codes,
+                                  float* scales, int* status, cudaStream_t stream)
 {
     InvRopeQuantParams Q;
     Q.o = o;
     Q.pos = pos;
     Q.pos_minus = pos_is_ctx ? 1 : 0;
+    Q.row_seq = row_seq;
     Q.cos_sin = cos_sin;
     Q.max_pos = max_pos;
     Q.n_heads = n_heads;
@@ -119,7 +121,7 @@ extern "C" dsv4_status dsv4_inv_rope_fp8_quant(const dsv4_inv_rope_quant_args* a
         (reinterpret_cast<uintptr_t>(a->scales_dev) & 3))
         return DSV4_ERR_SHAPE;
     const cudaError_t e = launch_inv_rope_quant(static_cast<const uint16_t*>(a->o_dev), a->num_tokens, a->n_heads,
-                                                a->positions_dev, false, a->cos_sin_dev, a->max_pos,
+                                                a->positions_dev, false, nullptr, a->cos_sin_dev, a->max_pos,
                                                 static_cast<uint8_t*>(a->codes_dev), a->scales_dev, a->status_dev,
                                                 reinterpret_cast<cudaStream_t>(stream));
     if (e == cudaErrorInvalidValue) return DSV4_ERR_UNSUPPORTED;

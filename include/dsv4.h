@@ -277,7 +277,8 @@ dsv4_status dsv4_plan_set_kv_layout(dsv4_plan* plan, dsv4_kv_layout layout);
  *   bytes and a zero pad byte) or 128 (indexer).
  * positions_dev, seq_dev: int32 [num_tokens].  The tokens of one sequence in
  *   one call are adjacent in the token array with contiguous increasing
- *   positions (checked: DSV4_DEV_BAD_POSITION).
+ *   positions (checked: DSV4_DEV_BAD_POSITION).  A row with sequence and
+ *   position -1 is padding and skipped.
  * ape_dev: fp32 [r][coff*d];  rms_weight_dev: fp32 [d];
  * cos_sin_dev: fp32 [max_pos][64] (dsv4_rope_table layout).
  * state_dev: fp32 [num_seqs][coff*r][2*coff*d], a per-sequence ring: the row
@@ -331,7 +332,8 @@ dsv4_status dsv4_compress_insert_pair(const dsv4_compress_args* main_args, const
  * rows_dev: fp32 [num_rows][d] (d = 576, 128 or 512 by kind; DSV4_CACHE_V4
  * rows also serve as the FP8 SWA tokens of a DSV4_KV_V4 plan, slot = token
  * position); seq_dev, slot_dev:
- * int32 [num_rows] (sequence and logical slot of each row). */
+ * int32 [num_rows] (sequence and logical slot of each row; both -1: padding,
+ * skipped). */
 typedef struct dsv4_insert_rows_args {
     int kind;
     int num_rows;
@@ -389,7 +391,8 @@ typedef struct dsv4_indexer_args {
      * each query row (a prefill query token of position ctx_len[b] - 1 takes
      * its sequence's row).  bt_rows: the block table's row count, which every
      * row_seq value must stay below (checked: DSV4_DEV_BAD_INDEX, the row
-     * then reads row 0). */
+     * then reads row 0).  A row with row_seq -1 and ctx_len 0 is padding: it
+     * selects nothing (length 0). */
     const int* row_seq_dev;
     int bt_rows;
 } dsv4_indexer_args;
@@ -462,7 +465,8 @@ typedef struct dsv4_mla_args {
     float* lse_dev;
     int* status_dev;
     /* As in dsv4_indexer_args: NULL for decode; else the block-table row
-     * (of both tables, bt_rows rows each) of each query row. */
+     * (of both tables, bt_rows rows each) of each query row.  A padding row's
+     * outputs, lse, codes and scales are left as they were. */
     const int* row_seq_dev;
     int bt_rows;
     /* DSV4_KV_V4 plans only, optional (NULL: not produced): the attention
@@ -568,7 +572,7 @@ dsv4_status dsv4_dequant_gather(const dsv4_gather_args* args, dsv4_stream_t stre
  * gather_len)) of its sequence row_seq_dev[t]; out_len_dev[t] is the count
  * and the rest of the row is -1.  A window token outside the gathered run, a
  * sequence out of range or an output row too short sets DSV4_DEV_BAD_INDEX
- * and out_len -1. */
+ * and out_len -1; a token with sequence and position -1 is padding: out_len 0. */
 typedef struct dsv4_combine_args {
     const int* topk_dev;           /* int32 [num_tokens][topk_stride] (logical slots, -1 padding) */
     int topk_stride;
@@ -631,7 +635,10 @@ dsv4_status dsv4_stream_gate(const dsv4_gate_args* args, dsv4_stream_t stream);
  *   token i of s, at row t = offsets[s] + i:  positions[t] = c + i,
  *     seqs[t] = s, row_ctx[t] = c + i + 1 (the ctx_len that the indexer and
  *     the prefill attention take for a query row).
- *   Rows t >= offsets[S] get position -1, sequence -1, row_ctx 0 and slot -1.
+ *   Rows t >= offsets[S] get position -1, sequence -1, row_ctx 0 and slot -1:
+ *     padding, which a step captured for more rows than it has tokens runs
+ *     on.  The calls that take rows skip it without a status bit (each says
+ *     which rows those are); any other row without a sequence is an error.
  * Each cache group (ratio r: tokens per entry; window w, 0 = none) has pages
  *   pages(x) = ceil(floor(x / r) / 64)        pages that x tokens' entries fill
  *   lo(x)    = w ? max(0, x - w + 1) / 64 : 0 first page a query at x reads

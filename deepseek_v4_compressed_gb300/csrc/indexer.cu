@@ -444,11 +444,11 @@ indexer_logits_tc(const __grid_constant__ CUtensorMap tm_cache, const __grid_con
     // the query row's block-table row (prefill rows map to their sequence's)
     auto seq_of_row = [&]() {
         int sq = b;
-        if (P.row_seq) {
+        // a row without slots reads no table (padding is such a row)
+        if (P.row_seq && n_my > 0) {
             sq = P.row_seq[b];
             if (sq < 0 || sq >= P.bt_rows) {
-                // (a padding row reads nothing: it has no slots)
-                if (lane == 0 && !padding_row(sq, P.ctx_len[b] - 1)) flag(P.status, DSV4_DEV_BAD_INDEX);
+                if (lane == 0) flag(P.status, DSV4_DEV_BAD_INDEX);
                 sq = 0;
             }
         }

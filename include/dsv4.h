@@ -391,8 +391,8 @@ typedef struct dsv4_indexer_args {
      * each query row (a prefill query token of position ctx_len[b] - 1 takes
      * its sequence's row).  bt_rows: the block table's row count, which every
      * row_seq value must stay below (checked: DSV4_DEV_BAD_INDEX, the row
-     * then reads row 0).  A row with row_seq -1 and ctx_len 0 is padding: it
-     * selects nothing (length 0). */
+     * then reads row 0).  A row without slots reads none: padding, row_seq -1
+     * and ctx_len 0, selects nothing (length 0). */
     const int* row_seq_dev;
     int bt_rows;
 } dsv4_indexer_args;

@@ -5,6 +5,8 @@
 //   out[t][g][j] = sum_b xs[t][g][b] ws[g][j / 128][b] sum_{i in b} x w
 #include <limits.h>
 
+#include <atomic>
+
 #include <cuda_fp16.h>
 
 #include "dsv4_common.cuh"
@@ -1003,12 +1005,65 @@ static dsv4_status launch_err(cudaError_t e)
     return DSV4_ERR_CUDA;
 }
 
-// CTAs that share the blocks of k of one tile: twice as many while every CTA
-// still has a place at once (two an SM) and a block.
+// k = 0: sums of nothing.  16 lanes per output row and 128 columns.
+template <int OUT>
+__global__ void __launch_bounds__(256) fp8_matmul_empty_kernel(const __grid_constant__ MatmulParams P)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int nb = (P.N + 127) / 128, lane = threadIdx.x & 31;
+    const long long rows = static_cast<long long>(P.T) * P.G * nb;
+    const float4 zero[2] = {};
+    for (long long i0 = blockIdx.x * 16ll + (threadIdx.x >> 5) * 2; i0 < rows; i0 += gridDim.x * 16ll) {
+        const long long i = i0 + (lane >> 4);
+        store_block<OUT>(P, i < rows, static_cast<int>(i / nb / P.G), static_cast<int>(i / nb % P.G),
+                    static_cast<int>(i % nb), lane & 15, zero, false);
+    }
+    __threadfence();
+}
+
+// Clusters of 2, 4 or 8 of the few-token kernel's CTAs (two an SM) that the current
+// device has room for at once: a cluster stays within a group of SMs, which leaves
+// fewer than there are places for CTAs (152, 74 and 36 on this GPU).
+static int clusters_at_once(int size)
+{
+    static std::atomic<int> known[64][4];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 2 * sm_count() / size;
+    std::atomic<int>& n = known[dev][size / 4 + 1];
+    if (n.load() > 0) return n.load();
+    // of a kernel without tensor memory: for those that use some the query counts one
+    // CTA an SM, also where two run (the times of all three few-token kernels jump at
+    // 37 clusters of 8 and 75 of 4)
+    const auto kernel = fp8_matmul_empty_kernel<DSV4_BF16>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size, 1, 1);
+    cfg.blockDim = dim3(kStThreads, 1, 1);
+    cfg.dynamicSmemBytes = 108 * 1024;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int most = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 108 * 1024) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&most, kernel, &cfg) != cudaSuccess || most < 1) {
+        (void)cudaGetLastError();
+        return 2 * sm_count() / size;
+    }
+    n.store(most);
+    return most;
+}
+
+// CTAs that share the blocks of k of one tile: twice as many while every tile's
+// cluster still has a place at once and every CTA a block.  (With two CTAs an SM
+// counted instead, the last of 37 or 38 and 75 or 76 tiles' clusters ran behind the
+// others: 32 tokens, k = 4096, 37 tiles 11.4 us, 75 tiles 15.3.)
 static int stream_split(long long tiles, int kblocks)
 {
     int split = 1;
-    while (split < 8 && tiles * split * 2 <= 2 * sm_count() && split * 2 <= kblocks) split *= 2;
+    while (split < 8 && split * 2 <= kblocks && tiles <= clusters_at_once(split * 2)) split *= 2;
     return split;
 }
 
@@ -1123,22 +1178,6 @@ static dsv4_status launch_pair(const MatmulParams& P, bool x_shared, bool w_shar
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return launch_err(cudaLaunchKernelEx(&cfg, fp8_matmul_pair_kernel<OUT, NC>, tx, tw, to, S));
-}
-
-// k = 0: sums of nothing.  16 lanes per output row and 128 columns.
-template <int OUT>
-__global__ void __launch_bounds__(256) fp8_matmul_empty_kernel(const __grid_constant__ MatmulParams P)
-{
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int nb = (P.N + 127) / 128, lane = threadIdx.x & 31;
-    const long long rows = static_cast<long long>(P.T) * P.G * nb;
-    const float4 zero[2] = {};
-    for (long long i0 = blockIdx.x * 16ll + (threadIdx.x >> 5) * 2; i0 < rows; i0 += gridDim.x * 16ll) {
-        const long long i = i0 + (lane >> 4);
-        store_block<OUT>(P, i < rows, static_cast<int>(i / nb / P.G), static_cast<int>(i / nb % P.G),
-                    static_cast<int>(i % nb), lane & 15, zero, false);
-    }
-    __threadfence();
 }
 
 template <int OUT>

@@ -10,9 +10,9 @@
 // the sums, the tables' old entries; who is done helps with the rest.
 // Small batches are bound by latency: the lengths, the sums, the pages, each
 // read behind the last, and the code itself, fetched anew by every launch (32
-// sequences 4.5 us; with the counting loop over the groups unrolled 4.8 us).
+// sequences 4.7 us; 0.3 us more with the counting loop over the groups unrolled).
 // Large ones by issuing instructions: the sums that every CTA repeats and the
-// rules of each row (2048 sequences of up to 128K tokens, three groups: 13.9 us,
+// rules of each row (2048 sequences of up to 128K tokens, three groups: 14.2 us,
 // where writing the tables and reading the pages held takes 4.6 us).
 #include <limits.h>
 

@@ -762,7 +762,8 @@ dsv4_status dsv4_fp8_block_quant(const dsv4_fp8_quant_args* args, dsv4_stream_t 
  * output column j:
  *   out[t][g][j] = sum_b xs[t][g][b] * ws[g][j / 128][b] *
  *                  sum_{i in block b} x[t][g][i] * w[g][j][i]
- * over the 128-wide blocks b of k (the last may be partly filled).  Products
+ * over the 128-wide blocks b of k (the last may be partly filled), the two
+ * scales multiplied first, in fp32.  Products
  * of a block are exact and summed in fp32 on the tensor cores, blocks are
  * summed in fp32; the result is rounded once to out_type, in a fixed order of
  * operations (same inputs, same bits).  With out_type DSV4_E4M3 the fp32

@@ -638,7 +638,8 @@ dsv4_status dsv4_stream_gate(const dsv4_gate_args* args, dsv4_stream_t stream);
  *   Rows t >= offsets[S] get position -1, sequence -1, row_ctx 0 and slot -1:
  *     padding, which a step captured for more rows than it has tokens runs
  *     on.  The calls that take rows skip it without a status bit (each says
- *     which rows those are); any other row without a sequence is an error.
+ *     which rows those are; dsv4_inv_rope_fp8_quant on its own, which sees
+ *     positions only, does not); any other row without a sequence is an error.
  * Each cache group (ratio r: tokens per entry; window w, 0 = none) has pages
  *   pages(x) = ceil(floor(x / r) / 64)        pages that x tokens' entries fill
  *   lo(x)    = w ? max(0, x - w + 1) / 64 : 0 first page a query at x reads
